@@ -15,10 +15,10 @@
 //
 // The e4m3 parts of a query or a weight are columns side by side: a product
 // of 48 columns takes the tensor cores no longer than one of 16 (46 clocks), so
-// three parts cost what one does, and their results are added as they are read: 4 streams of some
-// 100 k tokens went from 210 to 165 us.  The two bf16 parts of a weight stay one after the other into one
-// sum, as in the window kernel, so that a window's rows have a step's bits; their copies take longer than
-// the products anyway.
+// three parts cost what one does, and their results are added as they are read.  So are the two 16-bit parts of
+// a weight for heads of up to 128 elements (64 uneven streams: 67 us fp16, 69 bf16; one after the other into one sum
+// 80).  For 256 the window kernel has no room in TMEM for two sums, and its rows have a step's bits, so there they are
+// one after the other.
 #pragma once
 
 #include "gdn_attn_join.cuh"
@@ -83,9 +83,9 @@ __device__ __forceinline__ void step_weights_of(AttnShared &sh, StepShared &st, 
     // the weights of the tile before last have been read
     if (it >= 2) attn_wait(sh, &sh.ofull[it & 1], ((it >> 1) - 1) & 1, err);
     // as the second operand: column j's keys in swizzled rows of 128 bytes
+    if constexpr (KV == GDN_E4M3) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        if constexpr (KV == GDN_E4M3) {
+        for (int j = 0; j < W; ++j) {
             uint8_t *dst = to + j * 128 + ((uint32_t)key ^ ((uint32_t)(j & 7) << 4));
             float x = t[j];
 #pragma unroll
@@ -94,31 +94,30 @@ __device__ __forceinline__ void step_weights_of(AttnShared &sh, StepShared &st, 
                 dst[q * N * 128] = (uint8_t)b;
                 x = __fsub_rn(x, Elem<GDN_E4M3>::unpack2(b).x);
             }
-        } else {
-            uint8_t *dst = to + ((key >> 6) * Parts::kWeight * N + j) * 128 + ((uint32_t)(key & 63) * 2 ^ ((uint32_t)(j & 7) << 4));
-            if constexpr (ACT == GDN_BF16) {
-                const __nv_bfloat16 top = __float2bfloat16_rn(t[j]);
-                *reinterpret_cast<__nv_bfloat16 *>(dst) = top;
-                *reinterpret_cast<__nv_bfloat16 *>(dst + N * 128) =
-                    __float2bfloat16_rn(__fsub_rn(t[j], __bfloat162float(top)));
-            } else {
-                *reinterpret_cast<__half *>(dst) = __float2half_rn(t[j]);
-            }
+        }
+    } else {
+        uint8_t *rows = to + (key >> 6) * Parts::kWeight * N * 128;
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+            float x = t[j], y = t[j + 1];
+            const uint32_t top = first_parts<KV>(x, y), rest = Elem<KV>::pack2(x, y);
+            uint8_t *at0 = rows + j * 128 + ((uint32_t)(key & 63) * 2 ^ ((uint32_t)(j & 7) << 4));
+            uint8_t *at1 = rows + (j + 1) * 128 + ((uint32_t)(key & 63) * 2 ^ ((uint32_t)((j + 1) & 7) << 4));
+            *reinterpret_cast<uint16_t *>(at0) = (uint16_t)top;
+            *reinterpret_cast<uint16_t *>(at1) = (uint16_t)(top >> 16);
+            *reinterpret_cast<uint16_t *>(at0 + N * 128) = (uint16_t)rest;
+            *reinterpret_cast<uint16_t *>(at1 + N * 128) = (uint16_t)(rest >> 16);
         }
     }
     const float l = reduce_scatter<W>(t, lane);
     if (lane % (32 / W) == 0) st.wsum[it & 7][warp][lane / (32 / W)] = l;
 }
 
-// Parts of a weight that are columns side by side.
-template <int ACT, int KV>
-constexpr int kAside = KV == GDN_E4M3 ? AttnParts<ACT, KV>::kWeight : 1;
-
 template <int D, int ACT, int KV>
 __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __grid_constant__ AttnTcParams p) {
     using T = AttnTile<D, KV>;
     using Parts = AttnParts<ACT, KV>;
-    constexpr int N = kStepCols, kScores = N * Parts::kQuery, kSums = N * kAside<ACT, KV>;   // columns of the two products
+    constexpr int N = kStepCols, kScores = N * Parts::kQuery, kSums = N * kAside<D, ACT, KV>;   // columns of the two products
     constexpr uint32_t kNeed = 2 * kScores + 2 * T::kHalves * kSums;                         // of TMEM: each twice
     constexpr uint32_t kTmemCols = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     constexpr uint32_t kQueries = attn_queries<D, ACT, KV>(N);
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __
                     const uint32_t to = tmem_o + ((it & 1) * T::kHalves + half) * kSums;
                     auto value_step = [&](int k) {
 #pragma unroll
-                        for (int q = 0; q < Parts::kWeight / kAside<ACT, KV>; ++q)
+                        for (int q = 0; q < Parts::kWeight / kAside<D, ACT, KV>; ++q)
                             mma_ss<KV>(to, dv + k * ((T::kStepKeys / 8) * T::kGroup / 16),
                                        pi + (k / 4 * Parts::kWeight + q) * (N * 128 / 16) + k % 4 * 2, kDescO, k + q > 0);
                     };
@@ -220,7 +219,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __
             if (f.flags & kOpens) ++item;
             const float c = a.k_scale ? l2e * a.k_scale[f.head] : l2e;
             uint8_t *to = sp + (it & 1) * step_weights<ACT, KV>;
-            if (f.cols <= 8) step_weights_of<8, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
+            // (4 columns for themselves: 64 uneven streams of 4 query heads a key head 67 us, 80 with 8; over an 8-bit
+            // cache 70 and 85, but there the third copy of the code costs items of 6 columns 4 %: 177 to 184 us)
+            if (KV != GDN_E4M3 && f.cols <= 4) step_weights_of<4, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
+            else if (f.cols <= 8) step_weights_of<8, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
             else step_weights_of<16, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
             if (f.tail < kTileKeys)
                 clean_values<D, KV, 128>(p, sh, stages, v_block(it, n) * T::kPieces, f.tail, f.last, &sh.vbad[it & 7], tid);
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __
                     const uint32_t from = tmem_o + ((it & 1) * T::kHalves + half) * kSums + c8 + lane_base;
                     tmem_ld(from, o);
 #pragma unroll
-                    for (int q = 1; q < kAside<ACT, KV>; ++q) {
+                    for (int q = 1; q < kAside<D, ACT, KV>; ++q) {
                         float more[8];
                         tmem_ld(from + q * N, more);
 #pragma unroll

@@ -24,10 +24,10 @@
 // reach that layout: K by rows (K-major, 8-row groups a group apart), V
 // transposed (MN-major, blocks an atom apart, 8-key groups a group apart).
 //
-// Operands of few bits.  Weights are held in 16 bits for the second product:
-// bf16 in two parts (hi + lo, 2^-17 relative; a single bf16 part would be off
-// as much as the output's own rounding), fp16 scaled by 2^15 (2^-12 relative
-// down to weights of 2^-29).  An 8-bit cache is multiplied as it is: the
+// Operands of few bits.  Weights are held in two 16-bit parts for the second
+// product, as one would be off about as much as the output's own rounding
+// (fp16 2^-11, bf16 2^-8): bf16 2^-17 relative, fp16, scaled by 2^15, 2^-20
+// down to weights of 2^-19 and 2^-39 of the tile's largest at the least.  An 8-bit cache is multiplied as it is: the
 // tensor cores' e4m3 products are exact and summed in 32 bits (measured:
 // 2^-22 of the sum of magnitudes), so only q and the weights have to become sums of e4m3 parts of
 // 4 bits each, by powers of two: a bf16 q is two parts (8 bits), an fp16 q and a weight three
@@ -145,9 +145,14 @@ __device__ __forceinline__ float fold_sum(float A, float O, Fold f) { return __f
 template <int ACT, int KV>
 struct AttnParts {
     static constexpr int kQuery = KV != GDN_E4M3 ? 1 : ACT == GDN_BF16 ? 2 : 3;
-    static constexpr int kWeight = KV == GDN_E4M3 ? 3 : ACT == GDN_BF16 ? 2 : 1;
+    static constexpr int kWeight = KV == GDN_E4M3 ? 3 : 2;
     static constexpr float kShift = KV == GDN_E4M3 ? 8.0f : ACT == GDN_BF16 ? 0.0f : 15.0f;
 };
+
+// Parts of a weight whose products are summed apart and added as they are read (16-bit ones of 256 elements in one sum:
+// the window kernel's TMEM is full).  A window's rows have a step's bits, so the kernels go by the same rule.
+template <int D, int ACT, int KV>
+constexpr int kAside = KV == GDN_E4M3 || D <= 128 ? AttnParts<ACT, KV>::kWeight : 1;
 
 // A weight of the second product is 2^(s c - ref).
 template <int ACT, int KV>
@@ -155,6 +160,24 @@ __device__ __forceinline__ float ref_of(float m) {
     return __fsub_rn(zero_if_none(m), AttnParts<ACT, KV>::kShift);
 }
 __device__ __forceinline__ float weight_of(float s, float c, float ref) { return fast_exp2(__fmaf_rn(s, c, -ref)); }
+
+// The first 16-bit parts of two weights; what is left becomes the second.  An fp16 one is rounded down and what is
+// left is 2^-24 at least (0 for a weight of 0), so that both parts of an infinite value's product are infinities of one sign.
+template <int KV>
+__device__ __forceinline__ uint32_t first_parts(float &x, float &y) {
+    uint32_t two;
+    if constexpr (KV == GDN_FP16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(y), "f"(x));
+    else two = Elem<KV>::pack2(x, y);
+    const float2 top = Elem<KV>::unpack2(two);
+    if constexpr (KV == GDN_FP16) {
+        x = fmaxf(__fsub_rn(x, top.x), fminf(x, 5.9604644775390625e-08f));
+        y = fmaxf(__fsub_rn(y, top.y), fminf(y, 5.9604644775390625e-08f));
+    } else {
+        x = __fsub_rn(x, top.x);
+        y = __fsub_rn(y, top.y);
+    }
+    return two;
+}
 
 // ---- PTX pieces
 
@@ -212,10 +235,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *mbar) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
-    static_assert(N == 8 || N == 16, "columns");
+    static_assert(N == 4 || N == 8 || N == 16, "columns");
     uint32_t r[N];
     if constexpr (N == 16) {
         tc::tmem_ld16_nowait(addr, r);
+    } else if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
     } else {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])

@@ -45,6 +45,7 @@ template <int D, int ACT, int KV>
 __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(const __grid_constant__ AttnTcParams p) {
     using T = AttnTile<D, KV>;
     using Parts = AttnParts<ACT, KV>;
+    constexpr bool kApart = KV != GDN_E4M3 && kAside<D, ACT, KV> > 1;   // (the second part's product 128 columns on)
     constexpr int FN = D / 2;                             // sums a thread holds
     constexpr uint32_t kTmemCols = 512;                   // scores (then weights) twice, the product
     static_assert(sizeof(AttnShared) + sizeof(WindowShared) <= 227 * 1024 - kWindowSmem, "shared memory");
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
                         auto value_step = [&](int k) {
 #pragma unroll
                             for (int part = 0; part < Parts::kWeight; ++part)
-                                mma_ts<KV>(tmem_o + half * 128, w + k * T::kStepKeys + part * 8,
-                                           dv + k * ((T::kStepKeys / 8) * T::kGroup / 16), kDescO, k + part > 0);
+                                mma_ts<KV>(tmem_o + (half + (kApart ? part : 0)) * 128, w + k * T::kStepKeys + part * 8,
+                                           dv + k * ((T::kStepKeys / 8) * T::kGroup / 16), kDescO, k + (kApart ? 0 : part) > 0);
                         };
                         if (steps == T::kSteps) {
 #pragma unroll
@@ -218,11 +219,16 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
 #pragma unroll
                             for (int j = 0; j < T::kStepKeys / 2; ++j) {
                                 float &x = t[q * T::kStepKeys + 2 * j], &y = t[q * T::kStepKeys + 2 * j + 1];
-                                const uint32_t two = Elem<KV>::pack2(x, y);
-                                if (part + 1 < Parts::kWeight) {
-                                    const float2 top = Elem<KV>::unpack2(two);
-                                    x = __fsub_rn(x, top.x);
-                                    y = __fsub_rn(y, top.y);
+                                uint32_t two;
+                                if (KV != GDN_E4M3 && part == 0) {
+                                    two = first_parts<KV>(x, y);
+                                } else {
+                                    two = Elem<KV>::pack2(x, y);
+                                    if (part + 1 < Parts::kWeight) {
+                                        const float2 top = Elem<KV>::unpack2(two);
+                                        x = __fsub_rn(x, top.x);
+                                        y = __fsub_rn(y, top.y);
+                                    }
                                 }
                                 if constexpr (KV == GDN_E4M3) w[j / 2] = j & 1 ? w[j / 2] | two << 16 : two;
                                 else w[j] = two;
@@ -277,6 +283,12 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
                 for (int b = 0; b < FN; b += 16) {
                     float t[16];
                     tc::tmem_ld16(fold_t + b, t);
+                    if constexpr (kApart) {
+                        float more[16];
+                        tc::tmem_ld16(fold_t + 128 + b, more);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) t[j] = __fadd_rn(t[j], more[j]);
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float sum = fold_sum(A[b + j], t[j], e);

@@ -1,0 +1,85 @@
+"""How many bits of a weight and of a query reach the attention's results, on
+inputs where the results' own rounding does not hide it.
+
+A query is one element (1) and the scale 1, so a score is one element of a
+key and exact; a weight is then off by its parts' rounding (PART), by the
+score's two products with rounded constants and the exponential (some 2^-20
+for scores up to 4) and by the products' 32-bit sums (2^-22 of the sum of
+magnitudes): REST = 2^-18 covers the last three.  The values of the heavy tokens
+cancel in pairs, so that a result is far smaller than what it is a sum of.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_speculative_gb300 as gdn
+
+from attn_harness import E4M3, Pool, half_step
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+TYPES = [(BF, BF), (HF, HF), (BF, E4M3), (HF, E4M3)]
+REST = 2.0 ** -18
+
+
+def part(act, kv):
+    """Half a step of the parts that a weight is held in, and its error at least, relative to the largest weight."""
+    if kv is E4M3:
+        return 2.0 ** -13
+    return 2.0 ** -16 if act is BF else 2.0 ** -20
+
+
+def attend(pool, q, k, v, rows, scale=1.0, **scales):
+    dims = gdn.AttnDims(q.shape[1], k.shape[1], q.shape[2], scale=scale)
+    pages, dev = pool.dev(), lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    cache = {"k": k.cuda(), "v": v.cuda()} | {n: t.cuda() for n, t in scales.items()}
+    out = torch.full(q.shape, -77.0, dtype=q.dtype, device="cuda")
+    ws = torch.empty(gdn.attn_workspace_size(dims, pages, pool.S, q.shape[0]), dtype=torch.uint8, device="cuda")
+    if rows == 1:
+        gdn.attn_step(dims, cache, pages, dev(pool.slot), q.cuda(), out, ws)
+    else:
+        gdn.attn_window(dims, cache, pages, dev(pool.slot), dev(pool.row_ptr), q.cuda(), out, ws)
+    assert gdn.get_device_error() == 0
+    return out.double().cpu()
+
+
+def place(pool, token, shape, kv, fill=0.0):
+    """A pool that holds token[j] ([tokens, d]) at stream 0's tokens."""
+    x = torch.full(shape, fill)
+    at = pool.tokens(0)[: token.shape[0]]
+    x[at // pool.page_size, 0, at % pool.page_size] = token.float()
+    return x.to(kv)
+
+
+@pytest.mark.parametrize("rows", [1, 3])   # the step kernel; with 16 heads of 3 rows the window kernel
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_weights_keep_their_bits(act, kv, d, rows):
+    tokens, heavy, G = 333, 24, 16
+    pool = Pool([tokens], [rows], 16)
+    g = torch.Generator().manual_seed(d + rows)
+    score = torch.full((tokens + rows,), -24.0)
+    at = torch.randperm(tokens, generator=g)[:heavy]
+    score[at] = torch.rand((heavy,), generator=g) * 3
+    score = score.to(kv).double()
+    q = torch.zeros((rows, G, d))
+    q[..., 0] = 1.0
+    keys = torch.zeros((tokens + rows, d), dtype=torch.float64)
+    keys[:, 0] = score
+    p = torch.exp(score)
+    values = torch.zeros((tokens + rows, d), dtype=torch.float64)
+    for e in range(d):   # (rounding the second value leaves a result of half a step of it)
+        a, b = at[torch.randperm(heavy, generator=g)[:2]]
+        values[a, e] = 1.0
+        values[b, e] = float((-p[a] / p[b]).to(kv))
+    shape = (pool.n_pages, 1, 16, d)
+    out = attend(pool, q.to(act), place(pool, keys, shape, kv), place(pool, values, shape, kv), rows)
+    for i in range(rows):
+        w = p[: tokens + i + 1] / p[: tokens + i + 1].sum()
+        ref, size = w @ values[: tokens + i + 1], w @ values[: tokens + i + 1].abs()
+        bound = (part(act, kv) + REST) * size
+        bound = bound + half_step(act) * (ref.abs() + bound) + (2.0 ** -25 if act is HF else 0.0)
+        far = (out[i] - ref).abs()
+        assert (far <= bound).all(), f"row {i}: {float((far / bound).max()):.3g} times the bound"
