@@ -94,6 +94,11 @@ __device__ __forceinline__ void store_floats(void *dst, const float (&x)[N]) {
     }
 }
 
+// Two of the 8-bit type with more range (2^-16 to 57344) and 3 bits, nearest even, saturated.
+__device__ __forceinline__ uint16_t pack2_e5m2(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+}
+
 template <int T>
 constexpr int elem_bytes = T == GDN_E4M3 ? 1 : 2;
 

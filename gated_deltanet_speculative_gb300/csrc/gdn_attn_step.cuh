@@ -53,7 +53,7 @@ __device__ __forceinline__ void step_weights_of(AttnShared &sh, StepShared &st, 
     for (int q = 1; q < Parts::kQuery; ++q) {
         tmem_ld(scores + q * N + ((uint32_t)(warp * 32) << 16), r);
 #pragma unroll
-        for (int j = 0; j < W; ++j) t[j] = __fadd_rn(t[j], r[j]);
+        for (int j = 0; j < W; ++j) t[j] = __fmaf_rn(r[j], q == 1 ? 1.0f / Parts::kNext : 1.0f / (Parts::kNext * Parts::kNext), t[j]);
     }
     // the tile's largest score of each column
 #pragma unroll
@@ -85,14 +85,18 @@ __device__ __forceinline__ void step_weights_of(AttnShared &sh, StepShared &st, 
     // as the second operand: column j's keys in swizzled rows of 128 bytes
     if constexpr (KV == GDN_E4M3) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            uint8_t *dst = to + j * 128 + ((uint32_t)key ^ ((uint32_t)(j & 7) << 4));
-            float x = t[j];
+        for (int j = 0; j < W; j += 2) {
+            uint8_t *at0 = to + j * 128 + ((uint32_t)key ^ ((uint32_t)(j & 7) << 4));
+            uint8_t *at1 = to + (j + 1) * 128 + ((uint32_t)key ^ ((uint32_t)((j + 1) & 7) << 4));
+            float x = t[j], y = t[j + 1];
 #pragma unroll
             for (int q = 0; q < Parts::kWeight; ++q) {
-                const uint16_t b = Elem<GDN_E4M3>::pack2(x, 0.0f);
-                dst[q * N * 128] = (uint8_t)b;
-                x = __fsub_rn(x, Elem<GDN_E4M3>::unpack2(b).x);
+                const uint16_t two = Elem<GDN_E4M3>::pack2(x, y);
+                at0[q * N * 128] = (uint8_t)two;
+                at1[q * N * 128] = (uint8_t)(two >> 8);
+                const float2 top = Elem<GDN_E4M3>::unpack2(two);
+                x = __fmaf_rn(top.x, -Parts::kNext, x * Parts::kNext);   // (exact)
+                y = __fmaf_rn(top.y, -Parts::kNext, y * Parts::kNext);
             }
         }
     } else {
@@ -297,7 +301,8 @@ __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __
                         float more[8];
                         tmem_ld(from + q * N, more);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], more[j]);
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = __fmaf_rn(more[j], q == 1 ? 1.0f / Parts::kNext : 1.0f / (Parts::kNext * Parts::kNext), o[j]);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {

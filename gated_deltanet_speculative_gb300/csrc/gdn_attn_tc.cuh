@@ -30,8 +30,11 @@
 // down to weights of 2^-19 and 2^-39 of the tile's largest at the least.  An 8-bit cache is multiplied as it is: the
 // tensor cores' e4m3 products are exact and summed in 32 bits (measured:
 // 2^-22 of the sum of magnitudes), so only q and the weights have to become sums of e4m3 parts of
-// 4 bits each, by powers of two: a bf16 q is two parts (8 bits), an fp16 q and a weight three
-// (weights 2^-13 relative, 2^-19 of the tile's largest at the least).
+// 4 bits each: a bf16 q is two parts (8 bits), an fp16 q and a weight three
+// (2^-13 relative).  Where parts have sums of their own (steps) each is 2^5 times what it stands for relative to the
+// one before, so that small numbers keep their bits: 2^-26 of the tile's largest weight at the least, 2^-21 of a
+// query's largest element.  Where they share a sum (windows) the last part is e5m2, whose least number is 2^-16
+// instead of 2^-9: 2^-22 of the power of two above the tile's largest weight, 2^-21 of a query's largest element.
 // Sums are taken from the fp32 weights.
 #pragma once
 
@@ -146,6 +149,7 @@ template <int ACT, int KV>
 struct AttnParts {
     static constexpr int kQuery = KV != GDN_E4M3 ? 1 : ACT == GDN_BF16 ? 2 : 3;
     static constexpr int kWeight = KV == GDN_E4M3 ? 3 : 2;
+    static constexpr float kNext = KV == GDN_E4M3 ? 32.0f : 1.0f;   // scale of a part against the one before, if their sums are apart
     static constexpr float kShift = KV == GDN_E4M3 ? 8.0f : ACT == GDN_BF16 ? 0.0f : 15.0f;
 };
 
@@ -194,6 +198,7 @@ template <int BB>
 __device__ __forceinline__ uint32_t swizzled_piece(int r, int c) {
     return (uint32_t)((r & 7) * BB + (BB == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) * 16);
 }
+constexpr uint32_t kDescE5m2 = 1u << 7;   // the first operand is e5m2
 // Instruction descriptor: D in fp32, A and B of the operands' type, M = 128.
 template <int ACT, int KV>
 constexpr uint32_t kMmaDesc = (1u << 4) | (KV != GDN_E4M3 && ACT == GDN_BF16 ? (1u << 7) | (1u << 10) : 0u) | (8u << 24);
@@ -716,10 +721,12 @@ __device__ __forceinline__ void attn_copies(const AttnTcParams &p, AttnShared &s
 // blocks of a row's 128 bytes, in each block the rows, swizzled (as the copies of 16-bit queries lie).
 // A row is scaled by a power of two (its largest element to [128, 256)) and taken in e4m3 parts,
 // `part` bytes apart in blocks of `rows` rows; unscale[row] undoes the scale.  Rows from `cols` to `pad` are zeros.
-template <int D, int ACT, int THREADS>
+// APART: each part has sums of its own, else the last is e5m2.
+template <int D, int ACT, bool APART, int THREADS>
 __device__ __forceinline__ void load_queries(const AttnTcParams &p, const AttnWalk &w, int cols, int pad, uint8_t *sq,
                                              int rows, uint32_t part, float *unscale, int tid) {
     using T = AttnTile<D, GDN_E4M3>;
+    using Parts = AttnParts<ACT, GDN_E4M3>;
     const AttnParams &a = p.a;
     const char *q = a.q + (((size_t)w.x.r0 + w.i0) * a.Hq + w.head * a.G) * D * 2;
     // 8 lanes a row, a lane D / 8 consecutive elements
@@ -749,16 +756,21 @@ __device__ __forceinline__ void load_queries(const AttnTcParams &p, const AttnWa
 #pragma unroll
         for (int e = 0; e < kPer; ++e) x[e] = ldexpf(x[e], ex);
 #pragma unroll
-        for (int t = 0; t < AttnParts<ACT, GDN_E4M3>::kQuery; ++t) {
+        for (int t = 0; t < Parts::kQuery; ++t) {
 #pragma unroll
             for (int e = 0; e < kPer; e += 8) {
                 uint16_t b[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    if (!APART && t + 1 == Parts::kQuery) {
+                        b[j] = pack2_e5m2(x[e + 2 * j], x[e + 2 * j + 1]);
+                        continue;
+                    }
                     b[j] = Elem<GDN_E4M3>::pack2(x[e + 2 * j], x[e + 2 * j + 1]);
                     const float2 top = Elem<GDN_E4M3>::unpack2(b[j]);
-                    x[e + 2 * j] -= top.x;
-                    x[e + 2 * j + 1] -= top.y;
+                    const float next = APART ? Parts::kNext : 1.0f;
+                    x[e + 2 * j] = (x[e + 2 * j] - top.x) * next;
+                    x[e + 2 * j + 1] = (x[e + 2 * j + 1] - top.y) * next;
                 }
                 const int at = sub * kPer + e, piece = at / 16;
                 *reinterpret_cast<uint2 *>(sq + t * part + (piece / (T::kBlock / 16) * rows + (c & ~7)) * T::kBlock +
@@ -787,7 +799,7 @@ struct AttnRows {
 };
 
 // The queries' WARPS: the rows of each item of the run, BUFFERS items
-// ahead of the scores.  Those of 16 bits are copied as they are (a copy a block; rows behind the
+// ahead of the scores (two for steps, whose parts have sums of their own, one for windows).  Those of 16 bits are copied as they are (a copy a block; rows behind the
 // pass come along, are multiplied and seen by nothing).
 template <int D, int ACT, int KV, int BUFFERS, int WARPS, int ROWS>
 __device__ __forceinline__ void attn_queries_ahead(const AttnTcParams &p, AttnShared &sh, AttnRows<ROWS> &rows, uint8_t *sq,
@@ -811,7 +823,7 @@ __device__ __forceinline__ void attn_queries_ahead(const AttnTcParams &p, AttnSh
             }
         }
         if constexpr (KV == GDN_E4M3) {
-            load_queries<D, ACT, 32 * WARPS>(p, k, k.cols, pad, sq + b * buffer, block_rows, part, rows.unscale[item & 3], tid);
+            load_queries<D, ACT, BUFFERS == 2, 32 * WARPS>(p, k, k.cols, pad, sq + b * buffer, block_rows, part, rows.unscale[item & 3], tid);
             tc::fence_async_smem();
         }
         __syncwarp();

@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
                                                qb = dq + (part * query_part + (half * T::kBlocks + b) * nc * T::kBlock) / 16;
 #pragma unroll
                                 for (int kk = 0; kk < T::kBlock / 32; ++kk)
-                                    mma_ss<KV>(d, qb + kk * 2, kb + kk * 2, kDescS, half + t + kk > 0);
+                                    mma_ss<KV>(d, qb + kk * 2, kb + kk * 2,
+                                               KV == GDN_E4M3 && part + 1 == Parts::kQuery ? kDescS | kDescE5m2 : kDescS, half + t + kk > 0);
                             }
                             tc::mma_commit(&sh.empty[ring.at]);
                         }
@@ -118,7 +119,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
 #pragma unroll
                             for (int part = 0; part < Parts::kWeight; ++part)
                                 mma_ts<KV>(tmem_o + (half + (kApart ? part : 0)) * 128, w + k * T::kStepKeys + part * 8,
-                                           dv + k * ((T::kStepKeys / 8) * T::kGroup / 16), kDescO, k + (kApart ? 0 : part) > 0);
+                                           dv + k * ((T::kStepKeys / 8) * T::kGroup / 16),
+                                           KV == GDN_E4M3 && part + 1 == Parts::kWeight ? kDescO | kDescE5m2 : kDescO,
+                                           k + (kApart ? 0 : part) > 0);
                         };
                         if (steps == T::kSteps) {
 #pragma unroll
@@ -222,6 +225,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
                                 uint32_t two;
                                 if (KV != GDN_E4M3 && part == 0) {
                                     two = first_parts<KV>(x, y);
+                                } else if (KV == GDN_E4M3 && part + 1 == Parts::kWeight) {
+                                    two = pack2_e5m2(x, y);
                                 } else {
                                     two = Elem<KV>::pack2(x, y);
                                     if (part + 1 < Parts::kWeight) {

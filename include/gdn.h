@@ -578,7 +578,12 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  * its path to the root passes (trees); the window's keys and values stand at
  * tokens kv_len + index, where gdn_attn_prep wrote them:
  *     out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j)
- * with scores, softmax and sums in fp32, rounded once to act_type.
+ * with scores, softmax statistics and sums in fp32, rounded once to act_type.
+ * What the tensor cores multiply has fewer bits.  A weight p_j is held in parts:
+ * exact to 2^-17 (bf16 caches), 2^-20 (fp16) or 2^-13 (GDN_E4M3) of itself, or
+ * else, GDN_E4M3 only, to 2^-22 of the power of two above the largest weight of
+ * its 128 tokens (steps 2^-26).  An 8-bit cache is multiplied as it is, by queries
+ * in parts whose elements are off by at most 2^-21 of the query's largest.
  * gdn_attn_step: one row a stream, row s.  The others take row_ptr, parent
  * and n_rows as gdn_window and gdn_tree do, at most 16 rows a stream.
  *   q, out     device, act_type [R, Hq, d_head], contiguous
@@ -594,8 +599,7 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  * (n_rows too small for what row_ptr holds) set GDN_DERR_SPACE and nothing is written.
  * A stream's rows have the same bits alone and among others (steps among
  * steps, windows among windows), and with a 16-bit cache those of a chain
- * window the bits of steps with as many tokens.  An 8-bit cache is multiplied as it is: a weight is exact to 2^-13,
- * or to 2^-19 of the largest weight of its 128 tokens (0.5 to 1).
+ * window the bits of steps with as many tokens.
  * The calls are cooperative launches of one CTA an SM: on a device that does not give
  * the process all its SMs they fail with GDN_ECUDA.
  */

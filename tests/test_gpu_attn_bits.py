@@ -83,3 +83,59 @@ def test_weights_keep_their_bits(act, kv, d, rows):
         bound = bound + half_step(act) * (ref.abs() + bound) + (2.0 ** -25 if act is HF else 0.0)
         far = (out[i] - ref).abs()
         assert (far <= bound).all(), f"row {i}: {float((far / bound).max()):.3g} times the bound"
+
+
+# over an 8-bit cache: (weights' and queries' errors at the least) relative to the power of two above the largest
+# weight of a tile, and to the largest element of a query
+LEAST = {1: (2.0 ** -26, 2.0 ** -21), 3: (2.0 ** -22, 2.0 ** -21)}
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("act", [BF, HF])
+def test_small_weights_reach_the_sum(act, rows):
+    """One key with nearly all the weight and a value of 0, and 126 with 2^-18 of it each and values that agree."""
+    tokens, G, d = 127, 16, 64
+    pool = Pool([tokens], [rows], 16)
+    q = torch.zeros((rows, G, d))
+    q[..., 0] = 1.5781   # times -8: 2^-18.2
+    q = q.to(act)
+    keys, values = torch.zeros((tokens + rows, d)), torch.zeros((tokens + rows, d))
+    keys[1:, 0] = -8.0
+    values[1:tokens] = torch.linspace(0.5, 2.0, d).to(E4M3).float()
+    shape = (pool.n_pages, 1, 16, d)
+    out = attend(pool, q, place(pool, keys, shape, E4M3), place(pool, values, shape, E4M3), rows)
+    for i in range(rows):
+        score = keys[: tokens + i + 1, 0].double() * q[0, 0, 0].double()
+        w = torch.exp(score) / torch.exp(score).sum()
+        ref = w @ values[: tokens + i + 1].double()
+        bound = (2.0 ** -13 + REST) * ref + LEAST[rows][0] * values.double().sum(0)
+        bound = bound + half_step(act) * (ref + bound) + (2.0 ** -25 if act is HF else 0.0)
+        far = (out[i] - ref).abs()
+        assert (far <= bound).all(), f"row {i}: {float((far / bound).max()):.3g} times the bound"
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("act", [BF, HF])
+def test_small_elements_of_a_query_reach_the_scores(act, rows):
+    """A query with one large element that meets zeros, and small ones (2^-17.4 of it) that decide."""
+    tokens, G, d, large = 40, 16, 64, 1024.0
+    pool = Pool([tokens], [rows], 16)
+    small = torch.tensor(0.75 * 2.0 ** -10 * 8).to(act)
+    q = torch.full((rows, G, d), float(small)).to(act)
+    q[..., 0] = large
+    g = torch.Generator().manual_seed(3)
+    keys = torch.randint(-4, 5, (tokens + rows, 1), generator=g).float().expand(-1, d).clone()
+    keys[:, 0] = 0.0
+    values = torch.randn((tokens + rows, d), generator=g).to(E4M3).float()
+    shape = (pool.n_pages, 1, 16, d)
+    out = attend(pool, q, place(pool, keys, shape, E4M3), place(pool, values, shape, E4M3), rows)
+    for i in range(rows):
+        k, v = keys[: tokens + i + 1].double(), values[: tokens + i + 1].double()
+        score = k @ q[0, 0].double()
+        w = torch.softmax(score, 0)
+        off = LEAST[rows][1] * large * float(k.abs().sum(1).max()) + 2.0 ** -22 * float((k.abs() @ q[0, 0].double().abs()).max())
+        ref = w @ v
+        bound = (2 * off + 2.0 ** -13 + REST) * (w @ v.abs())
+        bound = bound + half_step(act) * (ref.abs() + bound)
+        far = (out[i] - ref).abs()
+        assert (far <= bound).all(), f"row {i}: {float((far / bound).max()):.3g} times the bound"
