@@ -608,12 +608,12 @@ def _pages(pages: dict, stack=True) -> c_pages:
     _need(kl, "kv_len", torch.int32, (n_slots,))
     free = pages["free_pages"]
     _need(free, "free_pages", torch.int32)
-    held = nf = None
+    held, nf = pages["n_held"], None
+    _need(held, "n_held", torch.int32, (n_slots,))
     if stack:
-        held, nf = pages["n_held"], pages["n_free"]
-        _need(held, "n_held", torch.int32, (n_slots,))
+        nf = pages["n_free"]
         _need(nf, "n_free", torch.int32, (1,))
-    return c_pages(bt.data_ptr(), kl.data_ptr(), held.data_ptr() if stack else None, free.data_ptr(),
+    return c_pages(bt.data_ptr(), kl.data_ptr(), held.data_ptr(), free.data_ptr(),
                    nf.data_ptr() if stack else None, n_slots, max_pages, free.numel(), int(pages["page_size"]))
 
 

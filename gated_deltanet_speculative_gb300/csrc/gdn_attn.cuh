@@ -11,7 +11,7 @@ struct AttnParams {
     char *out;                        // [R, Hq, D]
     char *k, *v;                      // [n_pages, Hkv, page_size, D]
     const float *k_scale, *v_scale;   // [Hkv] or nullptr
-    const int *block_table, *kv_len;
+    const int *block_table, *kv_len, *n_held;
     const int *slot, *row_ptr, *parent, *keep_row;   // row_ptr nullptr: one row a stream
     int n_slots, max_pages, n_pages, page_size, n_streams, n_rows;
     int Hq, Hkv, G;
@@ -38,7 +38,10 @@ __device__ __forceinline__ int attn_stream(const AttnParams &p, int s, AttnStrea
         if (x.r0 < 0 || r1 < x.r0 || r1 > p.n_rows || x.n > GDN_MAX_WINDOW) return GDN_DERR_ROWS;
     }
     x.len = p.kv_len[x.sl];
-    if (x.len < 0 || (long long)x.len + x.n > (long long)p.max_pages * p.page_size) return GDN_DERR_PAGES;
+    // (entries of the table behind the slot's own pages may name pages that others hold by now)
+    const int held = p.n_held[x.sl];
+    if (x.len < 0 || held < 0 || held > p.max_pages || (long long)x.len + x.n > (long long)held * p.page_size)
+        return GDN_DERR_PAGES;
     return 0;
 }
 

@@ -45,13 +45,13 @@ int check_pages_sizes(const gdn_pages *g) {
     return GDN_OK;
 }
 
-// The table and lengths (what every call that looks tokens up needs), or with `stack` all of it.
+// The table, lengths and held pages (what every call that looks tokens up needs), or with `stack` all of it.
 int check_pages(const gdn_pages *g, bool stack) {
     GDN_TRY(check_pages_sizes(g));
-    if (!g->block_table || !g->kv_len) return GDN_ENULL;
-    if (stack && (!g->n_held || !g->free_pages || !g->n_free)) return GDN_ENULL;
-    if (!aligned(g->block_table, 4) || !aligned(g->kv_len, 4)) return GDN_EALIGN;
-    if (stack && (!aligned(g->n_held, 4) || !aligned(g->free_pages, 4) || !aligned(g->n_free, 4))) return GDN_EALIGN;
+    if (!g->block_table || !g->kv_len || !g->n_held) return GDN_ENULL;
+    if (stack && (!g->free_pages || !g->n_free)) return GDN_ENULL;
+    if (!aligned(g->block_table, 4) || !aligned(g->kv_len, 4) || !aligned(g->n_held, 4)) return GDN_EALIGN;
+    if (stack && (!aligned(g->free_pages, 4) || !aligned(g->n_free, 4))) return GDN_EALIGN;
     return GDN_OK;
 }
 
@@ -112,6 +112,7 @@ int attn_params(gdn::AttnParams &p, const gdn_attn_dims *d, const gdn_attn_cache
     p.v_scale = c->v_scale;
     p.block_table = g->block_table;
     p.kv_len = g->kv_len;
+    p.n_held = g->n_held;
     p.slot = slot;
     attn_sizes(p, d, g, n_streams, n_rows);
     p.scale = d->scale;

@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(256) gdn_pages_commit_kernel(const PagesParams
         }
         more = __popc(path_bits(packed, kr - r0));
     }
-    const int len = p.kv_len[sl];
-    if (len < 0 || (long long)len + more > (long long)p.max_pages * p.page_size) {
+    const int len = p.kv_len[sl], held = p.n_held[sl];
+    if (len < 0 || held < 0 || held > p.max_pages || (long long)len + more > (long long)held * p.page_size) {
         raise_error(p.err, GDN_DERR_PAGES);
         return;
     }

@@ -535,7 +535,8 @@ int gdn_pages_plan(const gdn_pages *pages, const int32_t *slot, const int32_t *r
  * row_ptr[s] + 1 for chains (parent == NULL) and the node's depth for
  * trees; -1 leaves it.  keep_row and parent as gdn_commit and gdn_tree take
  * them; a bad one sets GDN_DERR_KEEP or GDN_DERR_PARENT and leaves the slot.
- * A length that would pass max_pages * page_size sets GDN_DERR_PAGES.
+ * A length that would pass the pages that the slot holds (n_held) sets
+ * GDN_DERR_PAGES and leaves it.
  * Trees also need gdn_attn_commit in every layer.
  */
 int gdn_pages_commit(const gdn_pages *pages, const int32_t *slot, const int32_t *row_ptr, const int32_t *parent,
@@ -595,7 +596,8 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  * A slot, row range, parent or length out of range sets its bit
  * (GDN_DERR_SLOT, _ROWS, _PARENT, _PAGES) and the stream's rows of out stay
  * unwritten, and so they do with GDN_DERR_PAGES if a page of its tokens is out of
- * range.  Lengths that need more workspace than gdn_attn_workspace_size() found
+ * range or its tokens and rows are more than the pages that its slot holds have room for
+ * (n_held: what stands behind them in the table may be another's by now).  Lengths that need more workspace than gdn_attn_workspace_size() found
  * (n_rows too small for what row_ptr holds) set GDN_DERR_SPACE and nothing is written.
  * A stream's rows have the same bits alone and among others (steps among
  * steps, windows among windows), and with a 16-bit cache those of a chain
@@ -623,7 +625,8 @@ size_t gdn_attn_workspace_size(const gdn_attn_dims *dims, const gdn_pages *pages
  * The window's other tokens keep what they held.  To be called per layer,
  * before gdn_pages_commit; chains need none.  keep_row[s] = -1 moves
  * nothing.  Arguments and errors as gdn_commit and gdn_tree; a page out of
- * range sets GDN_DERR_PAGES and the stream stays as it was.
+ * range, or tokens and rows behind the pages that the slot holds, set
+ * GDN_DERR_PAGES and the stream stays as it was.
  */
 int gdn_attn_commit(const gdn_attn_dims *dims, const gdn_attn_cache *cache, const gdn_pages *pages,
                     const int32_t *slot, const int32_t *row_ptr, const int32_t *parent, const int32_t *keep_row,

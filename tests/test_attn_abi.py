@@ -162,3 +162,13 @@ def test_inv_freq_schemes(d_rot):
     assert torch.equal(yarn[inside <= lo], plain[inside <= lo])
     assert torch.allclose(yarn[inside >= hi], plain[inside >= hi] / 16, rtol=1e-12)
     assert torch.all(turns[inside < lo] > 32) and torch.all(turns[inside > hi] < 1)
+
+
+def test_the_count_of_held_pages_is_needed_where_tokens_are_looked_up():
+    lib = gdn.load()
+    d, w, c, g, r = p = parts(n_held=None)
+    assert step(*p) == -2
+    assert lib.gdn_attn_commit(R(d), R(c), R(g), A16, A16, A16, A16, 2, 4, None) == -2
+    assert lib.gdn_pages_commit(R(g), A16, A16, None, A16, 2, 4, None) == -2
+    p = parts(n_held=MIS)
+    assert step(*p) == -3
