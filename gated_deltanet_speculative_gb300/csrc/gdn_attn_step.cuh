@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) gdn_attn_step_kernel(const __
             else if (f.cols <= 8) step_weights_of<8, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
             else step_weights_of<16, D, ACT, KV>(sh, st, f, item, c, tmem + (it & 1) * kScores, to, it, a.err);
             if (f.tail < kTileKeys)
-                clean_values<D, KV, 128>(p, sh, stages, v_block(it, n) * T::kPieces, f.tail, f.last, &sh.vbad[it & 7], tid);
+                clean_values<D, KV, 128>(p, sh, stages, it, n, f.tail, f.last, &sh.vbad[it & 7], tid);
             tc::fence_before_sync();
             tc::fence_async_smem();
             __syncwarp();

@@ -855,13 +855,18 @@ __device__ __forceinline__ void attn_queries_ahead(const AttnTcParams &p, AttnSh
 // is there, as far as the products go (value_steps()); so do elements of the window's own (key >= tail) that are not
 // finite, which are given back to the rows that see them.
 // (THREADS threads; vbad gets those rows' bits.)
+// The values have landed when their places' barriers say so, but a barrier can only be asked for the phase after its
+// last: with four or five places for pieces and two a tile, the use before may be the values of the tile before, not
+// there yet.  So the product of the tile before is waited for first.
 template <class T>
 __device__ __forceinline__ int value_steps(int last) { return min(T::kSteps, (last + T::kStepKeys - 1) / T::kStepKeys); }
 
 template <int D, int KV, int THREADS>
-__device__ __forceinline__ void clean_values(const AttnTcParams &p, AttnShared &sh, uint8_t *stages, int first_stage,
+__device__ __forceinline__ void clean_values(const AttnTcParams &p, AttnShared &sh, uint8_t *stages, int it, int n,
                                              int tail, int last, uint32_t *vbad, int tid) {
     using T = AttnTile<D, KV>;
+    const int first_stage = v_block(it, n) * T::kPieces;
+    if (it) attn_wait(sh, &sh.ofull[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1, p.a.err);
     constexpr int kRow = T::kBlocks * T::kBlock / 16;   // 16-byte pieces of a key's row
     const int end = value_steps<T>(last) * T::kStepKeys;
     const uint32_t round = (uint32_t)first_stage / (uint32_t)p.n_stages;

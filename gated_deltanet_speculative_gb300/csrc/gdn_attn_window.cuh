@@ -33,7 +33,7 @@ __device__ __forceinline__ void attn_clean(const AttnTcParams &p, AttnShared &sh
         attn_wait(sh, &sh.sfull[it & 1], (it >> 1) & 1, p.a.err);   // (its facts are known)
         const int tail = sh.facts[it % kAttnTiles].tail, last = sh.facts[it % kAttnTiles].last;
         if (tail < kTileKeys) {
-            clean_values<D, KV, 32>(p, sh, stages, v_block(it, n) * AttnTile<D, KV>::kPieces, tail, last, &sh.vbad[it & 7], lane);
+            clean_values<D, KV, 32>(p, sh, stages, it, n, tail, last, &sh.vbad[it & 7], lane);
             tc::fence_async_smem();
         }
         __syncwarp();
