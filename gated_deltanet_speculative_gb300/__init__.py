@@ -17,7 +17,7 @@ from . import synth  # noqa: F401
 from ._binding import (STEP_EARLY_STATE, AttnDims, Dims, GdnError, MAX_WINDOW, PREFILL_CHUNK,  # noqa: F401
                        PREFILL_NOALLOC_SCRATCH_BYTES,
                        attn_commit, attn_inv_freq, attn_prep, attn_step, attn_tree, attn_window, attn_workspace_size,
-                       commit, commit_replay, commit_replay_tree, commit_swap, debug_wait_timeout, get_device_error,
+                       commit, commit_replay, commit_replay_tree, commit_swap, debug_attn_wait_limit, debug_wait_timeout, get_device_error,
                        library_path, load, prefill, prepare, PreparedCall,
                        pages_commit, pages_plan, pages_release,
                        prefill_noalloc, prefill_workspace, prefill_workspace_size, step, step_ex, tree, tree_log, tree_pooled,

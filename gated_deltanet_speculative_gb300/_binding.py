@@ -123,6 +123,7 @@ _SIGS = {
     "gdn_attn_commit": [ctypes.POINTER(c_attn_dims), ctypes.POINTER(c_attn_cache), ctypes.POINTER(c_pages), _P, _P,
                         _P, _P, _I, _I, _P],
     "gdn_debug_wait_timeout": [ctypes.c_uint32, _P],
+    "gdn_debug_attn_wait_limit": [ctypes.c_uint32],
     "gdn_status_string": [ctypes.c_int],
     "gdn_get_device_error": [_P, ctypes.POINTER(ctypes.c_int32)],
 }
@@ -484,6 +485,13 @@ def debug_wait_timeout(polls: int = 1000, stream=None):
     it gives up after ``polls`` polls and sets the timeout bit (32) of the
     device error word."""
     _check("gdn_debug_wait_timeout", load().gdn_debug_wait_timeout(int(polls), _stream_ptr(stream)))
+
+
+def debug_attn_wait_limit(polls: int = 1 << 20):
+    """Every wait inside the attention calls that follow gives up after
+    ``polls`` polls, which sets the timeout bit (32) of the device error word
+    and leaves the results that depend on it unwritten.  No argument: the usual limit."""
+    _check("gdn_debug_attn_wait_limit", load().gdn_debug_attn_wait_limit(int(polls)))
 
 
 PREFILL_CHUNK = 64

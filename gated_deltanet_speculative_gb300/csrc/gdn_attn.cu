@@ -29,6 +29,14 @@ static unsigned long long call_token() {
     return next.fetch_add(1, std::memory_order_relaxed) % ((1ull << 38) - 1) + 1;
 }
 
+// Polls after which a wait of later calls gives up (gdn_debug_attn_wait_limit).
+static std::atomic<uint32_t> wait_limit{kAttnWaitLimit};
+bool attn_wait_limit(uint32_t polls) {
+    if (polls > kAttnWaitLimit) return false;
+    wait_limit.store(polls, std::memory_order_relaxed);
+    return true;
+}
+
 // Columns of a tile: the rows of a pass times G, 16 or a multiple of 32.
 static int columns_for(int rows, int G) {
     const int c = std::min(kAttnMaxCols, rows * G);
@@ -128,6 +136,7 @@ cudaError_t launch_attn(int D, int act, int kv, int max_rows, const AttnParams &
     p.n_slots = (int)std::min<size_t>((a.ws_bytes - l.base) / l.slot_bytes, UINT32_MAX / (l.slot_bytes / 16) - 1);
     p.counters = reinterpret_cast<unsigned long long *>(a.ws);
     p.token = call_token();
+    p.wait_limit = wait_limit.load(std::memory_order_relaxed);
     p.slots = a.ws + l.base;
     switch (D) {
         case 64: return launch_attn_tc_d64(act, kv, p, st);

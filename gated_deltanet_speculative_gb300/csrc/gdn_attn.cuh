@@ -49,6 +49,7 @@ __device__ __forceinline__ int attn_stream(const AttnParams &p, int s, AttnStrea
 int sm_count();
 // Bytes of workspace (include/gdn.h: gdn_attn_workspace_size).
 size_t attn_workspace(const AttnParams &sizes, int D);
+bool attn_wait_limit(uint32_t polls);
 cudaError_t launch_attn(int d_head, int act, int kv, int max_rows, const AttnParams &p, cudaStream_t st);
 
 }  // namespace gdn

@@ -304,6 +304,8 @@ int gdn_attn_tree(const gdn_attn_dims *dims, const gdn_attn_cache *cache, const 
                       workspace_bytes, stream);
 }
 
+int gdn_debug_attn_wait_limit(uint32_t polls) { return gdn::attn_wait_limit(polls) ? GDN_OK : GDN_EINVAL; }
+
 int gdn_attn_commit(const gdn_attn_dims *dims, const gdn_attn_cache *cache, const gdn_pages *pages,
                     const int32_t *slot, const int32_t *row_ptr, const int32_t *parent, const int32_t *keep_row,
                     int32_t n_streams, int32_t n_rows, void *stream) {

@@ -17,9 +17,9 @@ constexpr int kJoinSpans = 256;                         // spans at a time, at m
 constexpr int kJoinPieces = kJoinSpans * kSpanMost;
 
 // True once all tiles of the item have been counted in.
-__device__ __forceinline__ bool count_full(const unsigned long long *counter, int all, int *err) {
+__device__ __forceinline__ bool count_full(const unsigned long long *counter, int all, uint32_t limit, int *err) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kAttnWaitLimit; ++i) {
+    for (uint32_t i = 0; i < limit; ++i) {
         unsigned long long v;
         asm volatile("ld.acquire.gpu.u64 %0, [%1];" : "=l"(v) : "l"(counter) : "memory");
         if ((int)(v & ((1ull << kCountBits) - 1)) >= all) return true;
@@ -122,7 +122,7 @@ __device__ __forceinline__ bool attn_join(const AttnTcParams &p, AttnShared &sh,
                 } else if (!waited && tid == kJoinSpans) {
                     // meanwhile the item's other runs are waited for
                     flags[1] = flags[2] = 0;
-                    flags[0] = !count_full(p.counters + cut.run, cut.tiles, a.err);
+                    flags[0] = !count_full(p.counters + cut.run, cut.tiles, p.wait_limit, a.err);
                 }
                 waited = true;
                 __syncthreads();
@@ -283,7 +283,7 @@ __device__ __forceinline__ void attn_finish(const AttnTcParams &p, AttnShared &s
     // and out again, but not before all are in (an empty part has not waited); the last leaves 0 behind
     if (i >= 0 && i < n_cut) {
         unsigned long long *counter = p.counters + sh.cut[i].run;
-        if (!((waited >> i) & 1)) count_full(counter, sh.cut[i].tiles, p.a.err);
+        if (!((waited >> i) & 1)) count_full(counter, sh.cut[i].tiles, p.wait_limit, p.a.err);
         const unsigned long long sum = atomicAdd(counter, (unsigned long long)sh.cut[i].mine) + sh.cut[i].mine;
         if ((int)(sum & ((1ull << kCountBits) - 1)) == 2 * sh.cut[i].tiles) atomicExch(counter, 0ull);
     }

@@ -80,6 +80,7 @@ struct AttnTcParams {
     // weights) by column and the window rows whose values are not all finite, then the sums [D / 4][slot_cols][4]
     unsigned long long *counters;
     unsigned long long token;
+    uint32_t wait_limit;   // polls after which a wait gives up (kAttnWaitLimit but in tests)
     char *slots;
     uint32_t slot_bytes, stat_bytes;
 };
@@ -319,7 +320,7 @@ struct AttnWalk {
 };
 
 constexpr int kAttnStages = 16;
-constexpr int kAttnTiles = 32;   // facts of tiles that are kept: more than the copies can be ahead of the sums
+constexpr int kAttnTiles = 32;   // facts of tiles that are kept (a lane each at the start): more than the copies can be ahead of the sums
 
 // What the other parts of a CTA have to know of a tile, written by its copies' warp.
 struct AttnFacts {
@@ -338,7 +339,7 @@ struct AttnShared {
     uint64_t full[kAttnStages], empty[kAttnStages], sfull[2], pfull[2], ofull[2], ofree[2], qfull[2], qempty[2], done;
     AttnFacts facts[kAttnTiles];
     uint32_t vbad[8];          // by tile & 7: window rows whose values in the cache are not all finite
-    uint32_t tmem;
+    uint32_t tmem, wait_limit;
     int abort;
     int first_stream, n_table, first_tile, span0;
     AttnRuns runs;
@@ -350,7 +351,10 @@ struct AttnShared {
 
 // Wait for a phase; after one wait has given up every wait returns at once,
 // and the kernel runs to its end on whatever is there (all trip counts are
-// fixed beforehand), with the error raised and no result written.
+// fixed beforehand), with the error raised and no result written.  What is
+// there: a tile's facts may be those of the tile kAttnTiles before or zeros,
+// and two warps may see different ones, so no barrier of several warps
+// stands behind a condition on them.
 __device__ __forceinline__ bool mbar_done(uint64_t *mbar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -363,7 +367,7 @@ __device__ __forceinline__ bool mbar_done(uint64_t *mbar, uint32_t parity) {
 }
 __device__ __forceinline__ void attn_wait_on(AttnShared &sh, uint64_t *mbar, uint32_t parity, int *err) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kAttnWaitLimit; ++i) {
+    for (uint32_t i = 0, limit = sh.wait_limit; i < limit; ++i) {
         if (*(volatile int *)&sh.abort || mbar_done(mbar, parity)) return;
     }
     *(volatile int *)&sh.abort = 1;
@@ -508,8 +512,10 @@ __device__ __forceinline__ bool attn_prologue(const AttnTcParams &p, AttnShared 
             tc::mbar_init(&sh.qempty[lane], 1);
         }
         if (lane < 8) sh.vbad[lane] = 0;
+        sh.facts[lane] = AttnFacts{};   // (for parts whose first wait gives up)
         if (lane == 0) {
             sh.abort = 0;
+            sh.wait_limit = p.wait_limit;
             tc::mbar_init(&sh.done, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -645,7 +651,7 @@ __device__ __forceinline__ void attn_copies(const AttnTcParams &p, AttnShared &s
     if (lane == 0) sh.n_cut = 0;
     if (k.tile > 0 || k.tiles > n) cut_of(0, min(k.tiles - k.tile, n));
     AttnRing ring = {0, 1};   // (a fresh barrier counts as the phase before done)
-    int stage = 0;
+    int issued = 0;   // (none is issued after a wait has given up)
     struct Tile {
         int page, pages, group;   // this lane's page (a lane is a page), pages of the tile, first group of 8 keys in them
         AttnFacts facts;
@@ -680,7 +686,7 @@ __device__ __forceinline__ void attn_copies(const AttnTcParams &p, AttnShared &s
     };
     auto push = [&](const CUtensorMap *map, const Tile &t) {
 #pragma unroll
-        for (int half = 0; half < T::kPieces; ++half, ++stage, ring.next(p.n_stages)) {
+        for (int half = 0; half < T::kPieces; ++half, ring.next(p.n_stages)) {
             const int at = ring.at;
             attn_wait(sh, &sh.empty[at], ring.parity, a.err);
             __syncwarp();
@@ -690,6 +696,7 @@ __device__ __forceinline__ void attn_copies(const AttnTcParams &p, AttnShared &s
             if (lane < t.pages)
                 tma_load_5d(stages + at * T::kBytes + (lane << box_shift) / 8 * T::kGroup, map, half * T::kBlocks, t.group,
                             t.page, &sh.full[at]);
+            ++issued;
         }
     };
     // keys of tile it + 1, then values of tile it; a tile's pages are looked up a tile before they are copied
@@ -710,11 +717,9 @@ __device__ __forceinline__ void attn_copies(const AttnTcParams &p, AttnShared &s
     }
     __syncwarp();
     if (lane < sh.n_cut) count_from(p.counters + sh.cut[lane].run, p.token);
-    // copies still in flight (only after a wait gave up) land before the CTA ends
-    if (*(volatile int *)&sh.abort) {
-        for (int u = max(0, stage - p.n_stages); u < stage; ++u)
-            tc::mbar_wait(&sh.full[u % p.n_stages], (u / p.n_stages) & 1, 1u << 12);
-    }
+    // copies that nobody has waited for (after a wait gave up) land before the CTA goes on
+    for (int u = max(0, issued - p.n_stages); u < issued; ++u)
+        tc::mbar_wait(&sh.full[u % p.n_stages], (u / p.n_stages) & 1, kAttnWaitLimit);
 }
 
 // The item's query rows as the operand of an 8-bit cache, by THREADS threads:
@@ -843,10 +848,10 @@ __device__ __forceinline__ void attn_queries_ahead(const AttnTcParams &p, AttnSh
             walk_next(p, sh, k);
         }
     }
-    // copies still in flight (only after a wait gave up) land before the CTA ends
-    if (KV != GDN_E4M3 && tid < 32 && *(volatile int *)&sh.abort) {
+    // copies that nobody has waited for (after a wait gave up) land before the CTA goes on
+    if (KV != GDN_E4M3 && tid < 32) {
         for (int u = max(0, item - BUFFERS); u < item; ++u)
-            tc::mbar_wait(&sh.qfull[u % BUFFERS], (u / BUFFERS) & 1, 1u << 12);
+            tc::mbar_wait(&sh.qfull[u % BUFFERS], (u / BUFFERS) & 1, kAttnWaitLimit);
     }
 }
 

@@ -33,6 +33,9 @@ __device__ __forceinline__ void attn_clean(const AttnTcParams &p, AttnShared &sh
         attn_wait(sh, &sh.sfull[it & 1], (it >> 1) & 1, p.a.err);   // (its facts are known)
         const int tail = sh.facts[it % kAttnTiles].tail, last = sh.facts[it % kAttnTiles].last;
         if (tail < kTileKeys) {
+            // (the sums of the tile eight before have read theirs: their product's place was free for a later one)
+            if (lane == 0) sh.vbad[it & 7] = 0;
+            __syncwarp();
             clean_values<D, KV, 32>(p, sh, stages, it, n, tail, last, &sh.vbad[it & 7], lane);
             tc::fence_async_smem();
         }
@@ -304,10 +307,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1) gdn_attn_window_kernel(cons
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.ofree[0]);
-            if (f.tail < kTileKeys) {
-                named_barrier<2, 256>();
-                if (tid == 128) sh.vbad[it & 7] = 0;
-            }
             if (!last) continue;
             if (fresh) item_slot = f.slot;
             if (row < f.cols) {

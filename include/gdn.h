@@ -647,6 +647,16 @@ int gdn_attn_commit(const gdn_attn_dims *dims, const gdn_attn_cache *cache, cons
  */
 int gdn_debug_wait_timeout(uint32_t polls, void *stream);
 
+/*
+ * gdn_debug_attn_wait_limit -- a test hook of the same kind for the attention
+ * calls: every wait of the calls that follow in this process gives up after
+ * `polls` polls (at most 2^20, which is what they have otherwise; GDN_EINVAL
+ * above).  A call in which one gave up sets GDN_DERR_TIMEOUT, lets its copies
+ * land, writes no result that depends on the wait and leaves the workspace
+ * fit for the next call.
+ */
+int gdn_debug_attn_wait_limit(uint32_t polls);
+
 /* Text for a status code (static storage). */
 const char *gdn_status_string(int status);
 

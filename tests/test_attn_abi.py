@@ -172,3 +172,9 @@ def test_the_count_of_held_pages_is_needed_where_tokens_are_looked_up():
     assert lib.gdn_pages_commit(R(g), A16, A16, None, A16, 2, 4, None) == -2
     p = parts(n_held=MIS)
     assert step(*p) == -3
+
+
+def test_the_wait_limit_hook_bounds_its_polls():
+    lib = gdn.load()
+    assert lib.gdn_debug_attn_wait_limit((1 << 20) + 1) == -1
+    assert lib.gdn_debug_attn_wait_limit(5) == 0 and lib.gdn_debug_attn_wait_limit(1 << 20) == 0
