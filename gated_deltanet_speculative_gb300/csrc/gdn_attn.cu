@@ -22,11 +22,11 @@ int sm_count() {
     return n;
 }
 
-// A number that no earlier call of this process has, within 38 bits from a
+// A number that no earlier call of this process has, within 37 bits from a
 // random start: what an old workspace holds is taken for this call's counts only by an accident of that size.
 static unsigned long long call_token() {
     static std::atomic<unsigned long long> next{std::random_device{}() * 0x9E3779B97F4A7C15ull};
-    return next.fetch_add(1, std::memory_order_relaxed) % ((1ull << 38) - 1) + 1;
+    return next.fetch_add(1, std::memory_order_relaxed) % ((1ull << (64 - kCountBits)) - 1) + 1;
 }
 
 // Polls after which a wait of later calls gives up (gdn_debug_attn_wait_limit).

@@ -16,14 +16,17 @@ namespace gdn {
 constexpr int kJoinSpans = 256;                         // spans at a time, at most
 constexpr int kJoinPieces = kJoinSpans * kSpanMost;
 
-// True once all tiles of the item have been counted in.
-__device__ __forceinline__ bool count_full(const unsigned long long *counter, int all, uint32_t limit, int *err) {
+// True once all tiles of the item have been counted in.  A CTA that gives up, here or before, says so in the counter
+// before it counts (its tiles are counted in and out all the same), and nobody takes the item for complete any more.
+__device__ __forceinline__ bool count_full(unsigned long long *counter, int all, uint32_t limit, int *err) {
 #pragma unroll 1
     for (uint32_t i = 0; i < limit; ++i) {
         unsigned long long v;
         asm volatile("ld.acquire.gpu.u64 %0, [%1];" : "=l"(v) : "l"(counter) : "memory");
-        if ((int)(v & ((1ull << kCountBits) - 1)) >= all) return true;
+        if (v & kGaveUp) break;
+        if (count_of(v) >= all) return true;
     }
+    atomicOr(counter, kGaveUp);
     raise_error(err, GDN_DERR_TIMEOUT);
     return false;
 }
@@ -270,6 +273,7 @@ template <int D, int ACT, int KV, int T, bool STAGED>
 __device__ __forceinline__ void attn_finish(const AttnTcParams &p, AttnShared &sh, uint8_t *smem, int bytes) {
     // (all parts of the CTA are through)
     const int n_cut = sh.n_cut, i = threadIdx.x - kJoinSpans;
+    if (i >= 0 && i < n_cut && sh.abort) atomicOr(p.counters + sh.cut[i].run, kGaveUp);
     if (i >= 0 && i < n_cut)   // after the CTA's pieces
         asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p.counters + sh.cut[i].run),
                      "l"((unsigned long long)sh.cut[i].mine)
@@ -285,7 +289,7 @@ __device__ __forceinline__ void attn_finish(const AttnTcParams &p, AttnShared &s
         unsigned long long *counter = p.counters + sh.cut[i].run;
         if (!((waited >> i) & 1)) count_full(counter, sh.cut[i].tiles, p.wait_limit, p.a.err);
         const unsigned long long sum = atomicAdd(counter, (unsigned long long)sh.cut[i].mine) + sh.cut[i].mine;
-        if ((int)(sum & ((1ull << kCountBits) - 1)) == 2 * sh.cut[i].tiles) atomicExch(counter, 0ull);
+        if (count_of(sum) == 2 * sh.cut[i].tiles) atomicExch(counter, 0ull);
     }
 }
 

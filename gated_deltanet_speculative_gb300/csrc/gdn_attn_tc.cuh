@@ -619,7 +619,10 @@ __device__ __forceinline__ bool attn_prologue(const AttnTcParams &p, AttnShared 
     return true;
 }
 
-constexpr int kCountBits = 26;   // of a shared item's counter (its tiles, in and out); the others hold the token
+// A shared item's counter: its tiles, counted in and out (26 bits), whether a CTA gave up on it, and the token.
+constexpr int kCountBits = 27;
+constexpr unsigned long long kGaveUp = 1ull << (kCountBits - 1);
+__device__ __forceinline__ int count_of(unsigned long long v) { return (int)(v & (kGaveUp - 1)); }
 
 // An item's counter carries the token from here on; one that does not counts as 0.
 __device__ __forceinline__ void count_from(unsigned long long *counter, unsigned long long token) {
