@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepCtas) gdn_attn_prep_kernel(
                 for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], s);
             }
         }
-        store_floats<KV, 8>(pool + (cached + ((h << shift) * D + e0)) * elem_bytes<KV>, x);
+        store_floats<KV, 8>(pool + (cached + ((long long)(h << shift) * D + e0)) * elem_bytes<KV>, x);   // (a page may pass 2^31)
     };
 #pragma unroll 1
     while (row < p.n_rows) {

@@ -175,3 +175,22 @@ def test_prepared_call_in_a_graph():
         torch.cuda.synchronize()
         out.append((rows["q_out"], cache["k"], cache["v"]))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_a_page_of_more_than_two_to_the_31_elements():
+    """Key heads whose place in their page passes 31 bits (8-bit cache, one page of 2.1 GB each for k and v)."""
+    R, heads, d, page = 2, 8200, 256, 1024
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((R, heads, d), generator=g, device="cuda").to(BF) for _ in range(3))
+    cache = {n: torch.zeros((1, heads, page, d), dtype=torch.uint8, device="cuda").view(E4M3) for n in ("k", "v")}
+    place = torch.tensor([3, 1023], dtype=torch.int32, device="cuda")
+    gdn.attn_prep(gdn.AttnDims(heads, heads, d, d_rot=0), {}, cache, {"q": q, "k": k, "v": v, "q_out": torch.empty_like(q)},
+                  torch.zeros(R, dtype=torch.int32, device="cuda"), place)
+    assert gdn.get_device_error() == 0
+    for name, x in (("k", k), ("v", v)):
+        raw = cache[name].view(torch.uint8)[0]
+        want = x.float().to(E4M3).view(torch.uint8)
+        for r, at in enumerate(place.tolist()):
+            assert torch.equal(raw[:, at], want[r]), name
+            raw[:, at] = 0
+        assert not raw.any(), name
