@@ -601,7 +601,8 @@ def attn_inv_freq(d_rot: int, base: float = 10000.0, *, factor: float = 1.0, ntk
 
         def pair(turns):   # the (fractional) pair that turns so often within `trained` positions
             return d_rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), half - 1)
+        # (the ramp may end behind the last pair, where all pairs turn more than `slow` times)
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), d_rot - 1)
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         f = f * (1 - ramp) + f / by * ramp
     return f.to(device)

@@ -178,3 +178,25 @@ def test_the_wait_limit_hook_bounds_its_polls():
     lib = gdn.load()
     assert lib.gdn_debug_attn_wait_limit((1 << 20) + 1) == -1
     assert lib.gdn_debug_attn_wait_limit(5) == 0 and lib.gdn_debug_attn_wait_limit(1 << 20) == 0
+
+
+@pytest.mark.parametrize("d_rot,base,trained,fast,slow", [(64, 10000.0, 131072, 32, 1), (128, 10000.0, 1 << 20, 32, 1),
+                                                          (64, 10000.0, 4096, 32, 1), (64, 1e6, 32768, 32, 1),
+                                                          (16, 500.0, 131072, 64, 2)])
+def test_yarn_divides_only_pairs_that_turn_too_seldom(d_rot, base, trained, fast, slow):
+    """A pair that turns r times within the trained length is divided by the factor as the ramp between the pairs of
+    `fast` and `slow` turns says; one that turns more than `slow` times is never divided by all of it."""
+    import math
+    by = 4.0
+    plain = base ** (-2.0 * torch.arange(d_rot // 2, dtype=torch.float64) / d_rot)
+    yarn = gdn.attn_inv_freq(d_rot, base, yarn=(by, trained, fast, slow), device="cpu")
+    turns = plain * trained / (2 * math.pi)
+    # the pair that turns r times: base^(-2i/d_rot) trained / 2 pi = r
+    at = [d_rot / 2 * math.log(trained / (2 * math.pi * r)) / math.log(base) for r in (fast, slow)]
+    lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), d_rot - 1)
+    for i in range(d_rot // 2):
+        share = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+        want = float(plain[i]) * ((1 - share) + share / by)
+        assert abs(float(yarn[i]) - want) < 1e-12 * want
+        if turns[i] > slow and hi < d_rot - 1 and at[1] != math.ceil(at[1]):
+            assert yarn[i] > plain[i] / by * (1 + 1e-9)
