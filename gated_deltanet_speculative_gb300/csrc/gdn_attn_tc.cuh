@@ -26,7 +26,7 @@
 //
 // Operands of few bits.  Weights are held in two 16-bit parts for the second
 // product, as one would be off about as much as the output's own rounding
-// (fp16 2^-11, bf16 2^-8): bf16 2^-17 relative, fp16, scaled by 2^15, 2^-20
+// (fp16 2^-11, bf16 2^-8): bf16 2^-16 relative, fp16, scaled by 2^15, 2^-20
 // down to weights of 2^-19 and 2^-39 of the tile's largest at the least.  An 8-bit cache is multiplied as it is: the
 // tensor cores' e4m3 products are exact and summed in 32 bits (measured:
 // 2^-22 of the sum of magnitudes), so only q and the weights have to become sums of e4m3 parts of
@@ -166,20 +166,21 @@ __device__ __forceinline__ float ref_of(float m) {
 }
 __device__ __forceinline__ float weight_of(float s, float c, float ref) { return fast_exp2(__fmaf_rn(s, c, -ref)); }
 
-// The first 16-bit parts of two weights; what is left becomes the second.  An fp16 one is rounded down and what is
-// left is 2^-24 at least (0 for a weight of 0), so that both parts of an infinite value's product are infinities of one sign.
+// The first 16-bit parts of two weights; what is left becomes the second.  The first is rounded down and what is
+// left is not 0 either (fp16: 2^-24 at least; bf16: 2^-22 of the weight more) unless the weight is, so that both parts
+// of an infinite value's product are infinities of one sign.
 template <int KV>
 __device__ __forceinline__ uint32_t first_parts(float &x, float &y) {
     uint32_t two;
     if constexpr (KV == GDN_FP16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(y), "f"(x));
-    else two = Elem<KV>::pack2(x, y);
+    else two = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
     const float2 top = Elem<KV>::unpack2(two);
     if constexpr (KV == GDN_FP16) {
         x = fmaxf(__fsub_rn(x, top.x), fminf(x, 5.9604644775390625e-08f));
         y = fmaxf(__fsub_rn(y, top.y), fminf(y, 5.9604644775390625e-08f));
     } else {
-        x = __fsub_rn(x, top.x);
-        y = __fsub_rn(y, top.y);
+        x = __fmaf_rn(x, 2.384185791015625e-07f, __fsub_rn(x, top.x));
+        y = __fmaf_rn(y, 2.384185791015625e-07f, __fsub_rn(y, top.y));
     }
     return two;
 }

@@ -581,8 +581,8 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  *     out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j)
  * with scores, softmax statistics and sums in fp32, rounded once to act_type.
  * What the tensor cores multiply has fewer bits.  A weight p_j is held in parts:
- * exact to 2^-17 (bf16 caches), 2^-20 (fp16) or 2^-13 (GDN_E4M3) of itself, or
- * else, GDN_E4M3 only, to 2^-22 of the power of two above the largest weight of
+ * exact to 2^-16 (bf16 caches), 2^-20 (fp16) or 2^-13 (GDN_E4M3) of itself, or
+ * else to 2^-39 (fp16), 2^-22 (GDN_E4M3) of the power of two above the largest weight of
  * its 128 tokens (steps 2^-26).  An 8-bit cache is multiplied as it is, by queries
  * in parts whose elements are off by at most 2^-21 of the query's largest.
  * gdn_attn_step: one row a stream, row s.  The others take row_ptr, parent
@@ -592,7 +592,9 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  *              16-byte aligned; contents do not matter; GDN_EWORKSPACE if
  *              absent or too small.  Calls that may overlap need their own
  * Tokens that a row does not see do not reach it, whatever their keys hold
- * (infinities and NaN too); so do the values behind the stream's last row.
+ * (infinities and NaN too); so do the values behind the stream's last row.  An
+ * infinite value that it sees makes its element an infinity (no number if its weight
+ * is 0 in the cache's type or both signs meet).
  * A slot, row range, parent or length out of range sets its bit
  * (GDN_DERR_SLOT, _ROWS, _PARENT, _PAGES) and the stream's rows of out stay
  * unwritten, and so they do with GDN_DERR_PAGES if a page of its tokens is out of

@@ -139,3 +139,33 @@ def test_small_elements_of_a_query_reach_the_scores(act, rows):
         bound = bound + half_step(act) * (ref.abs() + bound)
         far = (out[i] - ref).abs()
         assert (far <= bound).all(), f"row {i}: {float((far / bound).max()):.3g} times the bound"
+
+
+@pytest.mark.parametrize("rows,G", [(1, 4), (1, 16), (16, 8)])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("act", [BF, HF])
+def test_infinite_committed_values_are_infinite_results(act, d, rows, G):
+    """A weight is not 0, so an infinite value of a token that all rows see makes its element an infinity of that sign;
+    both signs make it no number."""
+    tokens = 500
+    pool = Pool([tokens], [rows], 16)
+    g = torch.Generator().manual_seed(d)
+    shape = (pool.n_pages, 1, 16, d)
+    q, k = torch.randn((rows, G, d), generator=g).to(act), torch.randn((tokens + rows, d), generator=g).to(act)
+    v = torch.randn((tokens + rows, d), generator=g).to(act)
+    clean = attend(pool, q, place(pool, k, shape, act), place(pool, v, shape, act), rows, scale=0.25)
+    inf = float("inf")
+    v[3, 1] = v[200, 2] = v[499, 2] = v[130, 4] = inf
+    v[7, 3] = v[130, 5] = v[400, 4] = -inf
+    out = attend(pool, q, place(pool, k, shape, act), place(pool, v, shape, act), rows, scale=0.25)
+    # (an fp16 weight below 2^-39 of the largest of its 128 tokens may be 0)
+    score = torch.einsum("rgd,td->rgt", q.double(), k.double()) * 0.25
+    for e, at, sign in ((1, [3], inf), (2, [200, 499], inf), (3, [7], -inf), (5, [130], -inf)):
+        held = torch.ones((rows, G), dtype=torch.bool)
+        for t in at if act is HF else []:
+            tile = score[..., t // 128 * 128:min(t // 128 * 128 + 128, tokens)]
+            held &= score[..., t] - tile.amax(-1) > -38 * np.log(2.0)
+        assert (out[..., e][held] == sign).all() and held.any() and not out[..., e].isfinite().any()
+    assert out[..., 4].isnan().all()
+    rest = [e for e in range(d) if e not in (1, 2, 3, 4, 5)]
+    assert torch.equal(out[..., rest], clean[..., rest])
