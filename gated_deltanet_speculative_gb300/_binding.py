@@ -742,10 +742,13 @@ def attn_prep(dims: AttnDims, weights: dict, cache: dict, rows: dict, row_pos, r
                                               _stream_ptr(stream)))
 
 
-def attn_workspace_size(dims: AttnDims, pages: dict, n_streams: int, n_rows: int) -> int:
+def attn_workspace_size(dims: AttnDims, pages: dict, n_streams: int, n_rows: int, n_pages: int | None = None) -> int:
     """Bytes of scratch the attention calls need (0 for invalid sizes);
-    n_rows = n_streams for steps."""
+    n_rows = n_streams for steps.  ``n_pages``: the sum of the pages that the
+    streams hold, where rows of the table share pages (else the pool's)."""
     cp = _pages(pages, stack=False)
+    if n_pages is not None:
+        cp.n_pages = int(n_pages)
     return int(load().gdn_attn_workspace_size(ctypes.byref(dims.c()), ctypes.byref(cp), int(n_streams), int(n_rows)))
 
 

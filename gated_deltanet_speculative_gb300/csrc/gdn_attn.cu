@@ -49,14 +49,18 @@ struct AttnLayout {
     int slot_cols;
     long long slots;
 };
-// `r` window rows a pass, of at most `max_rows`: a stream takes ceil(rows / r) passes.
+// `r` window rows a pass, of at most `max_rows`: a stream takes ceil(rows / r) passes.  A pass over t tokens has
+// ceil(t / 512) spans, from 8192 tokens on 8 + ceil(t / 1024), so 1 + min(t / 512, 8 + t / 1024) at most: added up over
+// the passes, whose tokens are at most those of the table's rows, and those of the pool as often as a stream has passes
+// (pages that are in one row each; the kernels refuse lengths that need more).
 static AttnLayout attn_layout(int r, int max_rows, const AttnParams &a, int D, int grid) {
     AttnLayout l;
-    constexpr long long span = 4 * kTileKeys;   // the shortest
-    const long long streams = a.n_streams, passes = std::min({(long long)a.n_rows, streams * ((max_rows + r - 1) / r),
-                                                              streams + a.n_rows / r});
-    l.slots = passes * (((long long)a.max_pages * a.page_size + span - 1) / span) * a.Hkv +
-              (long long)grid * (kSpanMost - 1);
+    const long long streams = a.n_streams, each = (max_rows + r - 1) / r;
+    const long long passes = std::min({(long long)a.n_rows, streams * each, streams + a.n_rows / r});
+    const long long row = (long long)a.max_pages * a.page_size, pool = each * a.n_pages * a.page_size;
+    const long long row_spans = row <= 8192 ? (row + 511) / 512 : 8 + (row + 1023) / 1024;
+    const long long spans = std::min(passes * row_spans, passes + std::min(pool / 512, 8 * passes + pool / 1024));
+    l.slots = spans * a.Hkv + (long long)grid * (kSpanMost - 1);
     l.base = ((size_t)grid * 8 + 255) / 256 * 256;
     l.slot_cols = r * a.G;
     l.stat_bytes = ((size_t)(l.slot_cols + 1) * 8 + 15) / 16 * 16;

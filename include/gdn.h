@@ -599,8 +599,8 @@ int gdn_attn_prep(const gdn_attn_dims *dims, const gdn_attn_weights *w, const gd
  * (GDN_DERR_SLOT, _ROWS, _PARENT, _PAGES) and the stream's rows of out stay
  * unwritten, and so they do with GDN_DERR_PAGES if a page of its tokens is out of
  * range or its tokens and rows are more than the pages that its slot holds have room for
- * (n_held: what stands behind them in the table may be another's by now).  Lengths that need more workspace than gdn_attn_workspace_size() found
- * (n_rows too small for what row_ptr holds) set GDN_DERR_SPACE and nothing is written.
+ * (n_held: what stands behind them in the table may be another's by now).  Lengths that need more workspace than there is set GDN_DERR_SPACE and
+ * nothing is written (only tables that share pages have such, see gdn_attn_workspace_size).
  * A stream's rows have the same bits alone and among others (steps among
  * steps, windows among windows), and with a 16-bit cache those of a chain
  * window the bits of steps with as many tokens.
@@ -617,7 +617,13 @@ int gdn_attn_tree(const gdn_attn_dims *dims, const gdn_attn_cache *cache, const 
                   const int32_t *slot, const int32_t *row_ptr, const int32_t *parent, int32_t n_streams,
                   int32_t n_rows, const void *q, void *out, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace the attention calls need for these sizes (0 if invalid); n_rows = n_streams for steps. */
+/*
+ * Bytes of workspace the attention calls need for these sizes (0 if invalid);
+ * n_rows = n_streams for steps.  It grows with the tokens that the pool has
+ * pages for (or the table's rows, if that is less), each page in one row of the
+ * table.  Where rows share pages, size it with n_pages as the sum of the pages
+ * that the streams hold.
+ */
 size_t gdn_attn_workspace_size(const gdn_attn_dims *dims, const gdn_pages *pages, int32_t n_streams, int32_t n_rows);
 
 /*

@@ -200,3 +200,12 @@ def test_yarn_divides_only_pairs_that_turn_too_seldom(d_rot, base, trained, fast
         assert abs(float(yarn[i]) - want) < 1e-12 * want
         if turns[i] > slow and hi < d_rot - 1 and at[1] != math.ceil(at[1]):
             assert yarn[i] > plain[i] / by * (1 + 1e-9)
+
+
+def test_the_workspace_does_not_grow_with_the_table_where_the_pool_is_small():
+    size = lambda **over: gdn.load().gdn_attn_workspace_size(R(parts()[0]), R(parts(**over)[3]), 16, 256)  # noqa: E731
+    narrow = size(max_pages=512, n_pages=2000)
+    assert narrow == size(max_pages=1 << 16, n_pages=2000) > 0
+    assert size(max_pages=1 << 16, n_pages=1 << 20) > 20 * narrow
+    # 16 streams of a million tokens each, 24 heads on 4 of 256: pieces of 96 columns, 1032 a key head and stream
+    assert size(max_pages=1 << 16, n_pages=1 << 20) < 1.01 * (96 * 1024 + 1024) * (4 * 16 * 1040 + 160 * 7)
