@@ -5,9 +5,9 @@
 //
 // The angle of pair i at position p is p * inv_freq[i] radians.  Only its
 // fraction of a full turn matters, and in 64-bit fixed point that fraction is
-// exact: with t = frac(inv_freq / 2 pi) * 2^64 rounded to an integer, p * t
-// modulo 2^64 (one integer product) is the turn's fraction, 2^-64 * |p| off
-// at most.  Its upper 32 bits go through sincospif, so a position of a million is
+// exact: with t = frac(inv_freq / 2 pi) * 2^64 as an integer, off by 1 at
+// most, p * t modulo 2^64 (one integer product) is the turn's fraction,
+// 2^-64 * |p| off at most.  Its upper 32 bits go through sincospif, so a position of a million is
 // as exact as position one, where an fp32 product would be off by 0.06 rad.
 #pragma once
 
@@ -31,10 +31,12 @@ struct PrepParams {
 
 constexpr int kPrepThreads = 256, kPrepCtas = 3;
 
-// 2^64 * frac(inv_freq / 2 pi)
+// 2^64 * frac(inv_freq / 2 pi): the product and, from 1 / 2 pi in two parts, what it was rounded by
 __device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
-    const double f = inv_freq * 0.15915494309189533577;
-    return __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57, kTurn = 18446744073709551616.0;
+    const double x = fabs(inv_freq), f = x * kHi, rest = fma(x, kLo, fma(x, kHi, -f));
+    const unsigned long long t = __double2ull_rn((f - floor(f)) * kTurn) + (unsigned long long)__double2ll_rn(rest * kTurn);
+    return inv_freq < 0.0 ? 0ull - t : t;
 }
 
 // cos and sin of pos * (the turn), times gain
@@ -82,13 +84,14 @@ __global__ void __launch_bounds__(kPrepThreads, kPrepCtas) gdn_attn_prep_kernel(
         for (int j = 0; j < kAhead; ++j)
             if (base + j * kGroup + h0 < heads) raw[j] = *reinterpret_cast<const uint4 *>(from[j] + row * stride[j]);
     };
+    // (before the first row's loads: behind them it cost 4722 rows of 128-element heads 7 us, for want of registers)
+    const unsigned long long turn = tid < half ? turn_of(p.inv_freq[tid]) : 0;
     aim(0);
     uint4 next[kAhead];
     int row = blockIdx.x, base = 0, buffer = 0;
     bool kept = false;
     load(row, 0, next);
     int pos = p.row_pos[row], place = p.row_slot[row];
-    const unsigned long long turn = tid < half ? turn_of(p.inv_freq[tid]) : 0;
     if (tid < D / 8) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

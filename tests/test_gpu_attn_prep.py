@@ -7,7 +7,7 @@ import torch
 
 import gated_deltanet_speculative_gb300 as gdn
 
-from attn_harness import E4M3, check, prep_ref
+from attn_harness import E4M3, check, half_step, prep_ref
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -194,3 +194,37 @@ def test_a_page_of_more_than_two_to_the_31_elements():
             assert torch.equal(raw[:, at], want[r]), name
             raw[:, at] = 0
         assert not raw.any(), name
+
+
+def test_far_angles_to_the_last_bits():
+    """Near the last position, where a pair is almost back at its start: the sine is then far smaller than what an
+    angle made of 53 bits would be off by."""
+    from fractions import Fraction
+    import math
+    half, d = 32, 64
+    pi = Fraction(314159265358979323846264338327950288419716939937510, 10 ** 50)
+    rng = np.random.default_rng(7)
+    inv = np.sort(rng.uniform(0.05, 1.0, half))[::-1].copy()
+    p = np.arange(2 ** 31 - 65536, 2 ** 31, dtype=np.uint64)
+    pos, want = [], []
+    for f in inv.tolist():
+        turn = int(Fraction(f) / (2 * pi) * 2 ** 64) % 2 ** 64
+        off = (p * np.uint64(turn)).astype(np.int64)          # of a whole turn, 2^-64 of it each
+        at = int(p[np.argmin(np.abs(off.astype(np.float64)))])
+        part = Fraction(f) * at / (2 * pi)
+        part -= round(part)
+        pos.append(at)
+        want.append(math.sin(float(2 * pi * part)))
+    x = torch.zeros((half, 1, d), dtype=BF, device="cuda")
+    x[..., :half] = 1.0                                       # (1, 0) turns to (cos, sin)
+    rows = {"q": x, "k": x, "v": x, "q_out": torch.empty_like(x)}
+    cache = {n: torch.zeros((1, 1, 64, d), dtype=BF, device="cuda") for n in ("k", "v")}
+    gdn.attn_prep(gdn.AttnDims(1, 1, d), {"inv_freq": torch.from_numpy(inv).cuda()}, cache, rows,
+                  torch.tensor(pos, dtype=torch.int32, device="cuda"), torch.arange(half, dtype=torch.int32, device="cuda"))
+    assert gdn.get_device_error() == 0
+    got = torch.diagonal(rows["q_out"][:, 0, half:]).double().cpu()
+    want = torch.tensor(want, dtype=torch.float64)
+    # bf16's half step, the turn's 2^-64 and its upper 32 bits, and some 2^-21 of fp32
+    bound = want.abs() * (half_step(BF) + 2.0 ** -20) + 2 * math.pi * (2.0 ** -33 + 2.0 ** -32)
+    far = (got - want).abs()
+    assert (far <= bound).all(), f"{float((far / bound).max()):.3g} times the bound"
