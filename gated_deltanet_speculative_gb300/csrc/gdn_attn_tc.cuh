@@ -179,8 +179,8 @@ __device__ __forceinline__ uint32_t first_parts(float &x, float &y) {
         x = fmaxf(__fsub_rn(x, top.x), fminf(x, 5.9604644775390625e-08f));
         y = fmaxf(__fsub_rn(y, top.y), fminf(y, 5.9604644775390625e-08f));
     } else {
-        x = __fmaf_rn(x, 2.384185791015625e-07f, __fsub_rn(x, top.x));
-        y = __fmaf_rn(y, 2.384185791015625e-07f, __fsub_rn(y, top.y));
+        x = __fmaf_rn(x, 1.0000002384185791f, -top.x);
+        y = __fmaf_rn(y, 1.0000002384185791f, -top.y);
     }
     return two;
 }
@@ -340,7 +340,7 @@ struct AttnShared {
     uint64_t full[kAttnStages], empty[kAttnStages], sfull[2], pfull[2], ofull[2], ofree[2], qfull[2], qempty[2], done;
     AttnFacts facts[kAttnTiles];
     uint32_t vbad[8];          // by tile & 7: window rows whose values in the cache are not all finite
-    uint32_t tmem, wait_limit;
+    uint32_t tmem, first_poll;   // (a wait counts its polls from there to kAttnWaitLimit)
     int abort;
     int first_stream, n_table, first_tile, span0;
     AttnRuns runs;
@@ -368,7 +368,7 @@ __device__ __forceinline__ bool mbar_done(uint64_t *mbar, uint32_t parity) {
 }
 __device__ __forceinline__ void attn_wait_on(AttnShared &sh, uint64_t *mbar, uint32_t parity, int *err) {
 #pragma unroll 1
-    for (uint32_t i = 0, limit = sh.wait_limit; i < limit; ++i) {
+    for (uint32_t i = sh.first_poll; i < kAttnWaitLimit; ++i) {
         if (*(volatile int *)&sh.abort || mbar_done(mbar, parity)) return;
     }
     *(volatile int *)&sh.abort = 1;
@@ -516,7 +516,7 @@ __device__ __forceinline__ bool attn_prologue(const AttnTcParams &p, AttnShared 
         sh.facts[lane] = AttnFacts{};   // (for parts whose first wait gives up)
         if (lane == 0) {
             sh.abort = 0;
-            sh.wait_limit = p.wait_limit;
+            sh.first_poll = kAttnWaitLimit - p.wait_limit;
             tc::mbar_init(&sh.done, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
