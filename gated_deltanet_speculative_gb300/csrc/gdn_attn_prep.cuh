@@ -49,10 +49,10 @@ __device__ __forceinline__ float2 rotation(int pos, unsigned long long turn, flo
 
 // CTAs take rows in turn, kPrepCtas an SM; a lane has 8 consecutive elements of
 // a head, a warp 256 / D heads.  The next row (or the next four groups of heads of this one) is on its way
-// while one is worked on, and a pair's turn is a thread's for all its rows.  4722 rows of 48 heads of 128 take 30.8 us
+// while one is worked on, and a pair's turn is a thread's for all its rows.  4722 rows of 48 heads of 128 take 30.7 us
 // (3.8 TB/s): a row a CTA took 33.4, a head a warp with one load at a time 41, and four CTAs an SM, for which the
-// registers do not suffice, 40.9.  The instructions bound it: 180 for the 256 elements of a warp, 63 % of what the
-// SMs can issue.
+// registers do not suffice, 40.9.  No one limit is reached: 183 instructions for the 256 elements of a warp fill 62 % of
+// the issue slots, the copies have 56 % of their rate; a warp's loads, shuffles and stores wait for one another.
 template <int D, int ACT, int KV>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas) gdn_attn_prep_kernel(const PrepParams p) {
     constexpr int kLanes = D / 8, kGroup = kPrepThreads / kLanes, kAhead = 4;

@@ -9,9 +9,10 @@
 // products, weights (warpgroup 0), sums (warpgroup 1) and, an item ahead, the
 // queries.  Scores, weights and products have two buffers each.
 //
-// Measured: 64 streams of 8192 fp16 tokens (8 key heads of 128): 329 us, 6.5 TB/s,
-// the copies bind.  4 streams of some 110 k e4m3 tokens (4 heads of 256): 180 us, 5.1 TB/s, where a tile's copy
-// and the issue of its products take about as long.  One stream of 4722 bf16 tokens: 16.4 us, latency.
+// Measured: 64 streams of 8192 tokens of 16 bits (32 heads on 8 of 128): 345 us, 6.2 TB/s,
+// the copies bind.  4 streams of 65 to 131 k e4m3 tokens (24 heads on 4 of 256): 178 us, 5.2 TB/s, where a tile's copy
+// and the issue of its products take about as long (187 us with fp16 rows, whose queries are three parts).
+// One stream of 4722 bf16 tokens: 16.4 us, latency.
 //
 // The e4m3 parts of a query or a weight are columns side by side: a product
 // of 48 columns takes the tensor cores no longer than one of 16 (46 clocks), so

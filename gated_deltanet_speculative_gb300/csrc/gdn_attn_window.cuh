@@ -7,9 +7,11 @@
 // thread and half of the head each.  The parts run as in the step kernel;
 // scores have two buffers, the product one (TMEM is full).
 //
-// Measured: 16 streams x 16 rows over 512 to 8192 bf16 tokens (24 heads on 4 of 256): 88 us, 203 TFLOP/s,
-// 2.2 TB/s of cache beside 57 MB of pieces out and in; with 48 KB of queries
-// there is room for 1.25 tiles on the way.
+// Measured: 16 streams x 16 rows over 512 to 8192 bf16 tokens (24 heads on 4 of 256): 87 us, 205 TFLOP/s,
+// 2.2 TB/s of cache beside 57 MB of pieces out and in.  The chain within a tile binds, scores to weights to
+// product to sums: with equal lengths each further tile of a CTA takes 4.6 us (96 rows, heads of 256), 2.7
+// (64 rows of 128) or 3.1 (128 rows of 128), where its copies need 2.9 and 1.5.  At 128 registers a thread the kernels for
+// 256 elements spill 100 to 250 bytes, those for 64 and 128 16 to 28.
 #pragma once
 
 #include "gdn_attn_join.cuh"

@@ -435,6 +435,9 @@ int gdn_commit_replay_tree(const gdn_dims *dims, const gdn_cache *cache, const i
  *     gdn_attn_prep, gdn_attn_{step,window,tree}   per layer
  *     gdn_attn_commit                      per layer, after trees
  *     gdn_pages_commit                     once: the kept rows' lengths
+ * Prompts of any length are planned, prepared and committed the same way; the
+ * attention calls themselves take at most 16 rows a stream (a prompt's own
+ * attention has no call here but windows of 16 of its rows at a time).
  * The source pages name the parts (a paged cache, tree windows over it, an
  * 8-bit form of it, reductions that do not depend on the batch) and give no
  * formulas; those are written here.
@@ -560,8 +563,8 @@ int gdn_pages_release(const gdn_pages *pages, const int32_t *slot, int32_t n_str
  * eps) * (norm_offset + weight) (left out where the weight is NULL), their
  * leading d_rot elements are rotated, (a, b) -> (a cos t - b sin t, b cos t
  * + a sin t) * rot_gain with t = row_pos * inv_freq[i], and k and v are
- * written to the cache at row_slot.  All of it in fp32 (t exactly, modulo a
- * full turn), rounded once, to act_type for q_out and to kv_type for the
+ * written to the cache at row_slot.  All of it in fp32 (t to 2^-32 of a
+ * turn at any position), rounded once, to act_type for q_out and to kv_type for the
  * cache (GDN_E4M3: x / scale, to nearest even, saturated at +-448).
  *   row_pos, row_slot  device int32 [n_rows], as gdn_pages_plan writes them.
  *              row_slot -1: the row's k and v are not written; any other
