@@ -1,6 +1,8 @@
 // gdn_attn.cu -- launches of the attention over the paged cache.
 #include <algorithm>
 #include <atomic>
+#include <chrono>
+#include <cstdint>
 #include <random>
 
 #include "gdn_attn_tc.cuh"
@@ -22,10 +24,21 @@ int sm_count() {
     return n;
 }
 
+// Entropy where the system gives it (it throws where not, and the entries are C), else the clock and an address.
+static unsigned long long random_start() noexcept {
+    unsigned long long x;
+    try {
+        x = std::random_device{}();
+    } catch (...) {
+        x = (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() ^ (uintptr_t)&x;
+    }
+    return x * 0x9E3779B97F4A7C15ull;
+}
+
 // A number that no earlier call of this process has, within 37 bits from a
 // random start: what an old workspace holds is taken for this call's counts only by an accident of that size.
 static unsigned long long call_token() {
-    static std::atomic<unsigned long long> next{std::random_device{}() * 0x9E3779B97F4A7C15ull};
+    static std::atomic<unsigned long long> next{random_start()};
     return next.fetch_add(1, std::memory_order_relaxed) % ((1ull << (64 - kCountBits)) - 1) + 1;
 }
 
